@@ -160,7 +160,7 @@ append_q4_kernel(Q4Pages c, const T *__restrict__ K, int64_t k_stride, const T *
         }
     }
     __half sh, zh;
-    const bool ok = q4_params(mn, mx, sh, zh);
+    const bool ok = q4_params<sizeof(T) == 4>(mn, mx, sh, zh);
     const float s = __half2float(sh), zero = __half2float(zh);
     const float inv = !ok ? -1.0f : s > 0.0f ? __frcp_rn(s) : 0.0f;
     if (!ok && p.live) set_err(err, KVR_DEVERR_RANGE);
