@@ -658,7 +658,9 @@ size_t kvr_attend_q4_workspace_size(const kvr_q4_cache *cache, int B, int Lq, in
  * kv head g / (Hq/Hkv):
  *   out[b, t, g, :] = sum_{i <= N - Lq + t} softmax_i(scale * q . k_i) v_i
  * over the cached values k_i, v_i; a row without tokens (N - Lq + t < 0) is 0.
- * Sums are kept in fp32. A query row that is not finite gives NaN, and so may one
+ * Sums are kept in fp32: a score is off by less than 2^-17 of
+ * |scale| sum_c |q_c| (s code_c + |z|); channels of an fp32 query are held to 2^-22 of their
+ * own size and 2^-37 of the row's largest. A query row that is not finite gives NaN, and so may one
  * whose scores (times log2 e) pass fp32's range. Keys and values behind N, whatever
  * they hold, do not enter. A token's probability is held to 2^-36 of the row's
  * largest beside its own rounding.

@@ -10,14 +10,17 @@
 // A decode step has few query rows, so the 16-row side must be the cache: the
 // 128-row tiles of tcgen05 would be 94% padding, and its operands would have
 // to be written to shared memory as fp16, four times the bytes the codes have.
-// The codes enter as they lie. A nibble masked out of a 32-bit word is, read
-// as fp16, the denormal c * 2^-24 (low nibble of a half) or 16 c * 2^-24 (second
-// nibble), so 8 codes become 4 operand registers with one shift and four
-// LOP3. The factor 16 goes into the query (exactly: a power of two) or into the
-// output channel, 2^24 into the scales. The tensor core aligns a denormal
-// by its nominal exponent, which costs about 8 of the product's 24 bits: 2^-16
-// beside a bf16 output's 2^-8. For fp32 outputs (EXACT) the codes are
-// made normal numbers first, (0x6400 | c) - 1024, one more HADD2 per pair.
+// Codes are masked out of their words two at a time: 8 codes become 4 operand
+// registers with one shift and four LOP3. Every other pair is 16 times the code, and the factor goes
+// into the query (exactly: a power of two) or into the output channel.
+//   S: a logit's error counts as it is, however large the logit, so codes enter as normal
+//   numbers, (0x6400 | c) - 1024, one more HADD2 per pair. (A masked nibble as it lies is the
+//   denormal c * 2^-24. The tensor core aligns a denormal by its nominal exponent, which costs about 8 of the
+//   product's 24 bits beside the row's largest query channel: logits off by up to 3500 * 2^-24 of their magnitude,
+//   the sum of |q_c k_c|, where one channel outweighs the others, by 70 as it is. 128K tokens, bf16: 43.3 us, 40.9
+//   with denormals.)
+//   O: for bf16 outputs the codes are those denormals, in units of 2^-24: 2^-16 of the sum beside the
+//   output's 2^-8. For fp32 outputs (EXACT) they are normal numbers.
 // Scales and zeros stay outside the products with the codes:
 //   q . k   = sum over groups g of s_g (q . c)_g + z_g (sum of q over g)
 //   p . v_g = sum over tokens of (p s_g) c + p z_g
@@ -156,7 +159,7 @@ __device__ __forceinline__ void fma4(float4 &o, float f, const float4 &v)
 }
 
 // The state of one of WARPS warps for a unit, NT blocks of 8 query rows. Q2: queries as two
-// fp16 terms (fp32 queries). EXACT: fp32 outputs (codes as normal numbers,
+// fp16 terms (fp32 queries). EXACT: fp32 outputs (the values' codes as normal numbers,
 // probabilities times scales as two fp16 terms).
 template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     static constexpr int NG = D / 32, RT = 8 * NT;
@@ -168,7 +171,6 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     // measured to lose 5e-4 of the sum. EXACT adds every tile's sum in fp32
     // instead (32 FADD) and folds once, at the end.
     static constexpr int FOLD = EXACT ? INT32_MAX : 32;
-    static constexpr float KEXP = EXACT ? 0.0f : 24.0f;  // codes are in units of 2^-KEXP
 
     // Scores are kept as x with logit (log2) = x * kq, kq > 0. Probabilities are
     // 2^(x kq - ref) with ref = (largest x so far) kq - kExp: up to 2^14.
@@ -295,7 +297,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
             qz[t][0] = j == 0 ? part[0][0] : j == 1 ? part[1][0] : j == 2 ? part[2][0] : 0u;
             qz[t][1] = 0u;
         }
-        const int ke = (int)KEXP - up;  // -139 .. 138, in two factors
+        const int ke = -up;  // -139 .. 114, in two factors
         // (below 2^-110 all logits vanish: x is under 2^50, and a factor of 0 would make a masked
         // score's -inf a NaN)
         const float k = kscale == 0.0f ? 1.0f : fmaxf(kscale * pow2(ke >> 1) * pow2(ke - (ke >> 1)), 0x1p-110f);
@@ -405,13 +407,13 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                 float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 mma_f16(z, za, zb, za, zb, qz[t][0], qz[t][1]);
 #pragma unroll
-                for (int i = 0; i < 4; i++) x[t][h][i] = z[i] * (EXACT ? 64.0f : 64.0f * 0x1p-24f);
+                for (int i = 0; i < 4; i++) x[t][h][i] = z[i] * 64.0f;
             }
 #pragma unroll
             for (int gr = 0; gr < NG; gr++) {
                 uint32_t ra[4], rb[4];
-                unpack<EXACT>(wa[gr], ra);
-                unpack<EXACT>(wb[gr], rb);
+                unpack<true>(wa[gr], ra);
+                unpack<true>(wb[gr], rb);
                 const float2 sa2 = floats_of(ks[0][gr / 2]), sb2 = floats_of(ks[1][gr / 2]);
                 const float sa = (gr & 1) ? sa2.y : sa2.x, sb = (gr & 1) ? sb2.y : sb2.x;
 #pragma unroll
