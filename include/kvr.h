@@ -663,7 +663,9 @@ size_t kvr_attend_q4_workspace_size(const kvr_q4_cache *cache, int B, int Lq, in
  * own size and 2^-37 of the row's largest. A query row that is not finite gives NaN, and so may one
  * whose scores (times log2 e) pass fp32's range. Keys and values behind N, whatever
  * they hold, do not enter. A token's probability is held to 2^-36 of the row's
- * largest beside its own rounding.
+ * largest, P, beside its own rounding; its product with a scale of its values to 2^-36 P,
+ * and where the scales of a group are all under 2^-11 (KVR_F32: 2^-7) in 32 consecutive tokens of the
+ * list, or one is 2 or more, to 2^-38 of the row's largest such product among these tokens.
  *   q           device [B, Lq, Hq, d] of q_dtype, 16-byte aligned; row (b, t)
  *               starts at element (b * Lq + t) * q_stride, a multiple of 16
  *               bytes and at least Hq * d.

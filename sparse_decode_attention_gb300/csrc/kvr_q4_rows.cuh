@@ -484,20 +484,31 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
 #pragma unroll
                 for (int i = 0; i < 4; i++) over = fmaxf(over, y[t][h][i]);
         const bool raise = over > kExp + kSlack;
-        // scales of 2 and more, or none from 2^-11 on, want other units: the sign bit and the
-        // exponent's leading ones in the scales' OR (a lane whose tokens are masked says nothing)
-        uint32_t bits = 0;
+        // scales of 2 and more (or negative ones, or NaN), and a group whose scales are all under 2^-11
+        // (EXACT: 2^-7), want units of their own: the top bits of the scales' OR. A group of zeros alone, or of
+        // tokens that are masked, passes the first test and not the second.
+        constexpr uint32_t kLow = EXACT ? 0x2000u : 0x1000u;  // 2^-7, 2^-11 as fp16 bits
+        uint32_t bits[NG / 2], odd_bits = 0;
 #pragma unroll
-        for (int h = 0; h < H; h++)
+        for (int k = 0; k < NG / 2; k++) {
+            bits[k] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int h = 0; h < H; h++)
 #pragma unroll
-                for (int k = 0; k < NG / 2; k++) bits |= vs[h][i][k];
-        const bool tiny = (bits & 0xf000f000u) == 0u;
-        bool odd = (bits & 0xc000c000u) != 0u || (tiny && (!MASKED || bits != 0u));
+                for (int i = 0; i < 4; i++) bits[k] |= vs[h][i][k];
+            const uint32_t top = bits[k] & (0x10001u * (0x10000u - kLow));
+            odd_bits |= ((bits[k] << 1) & 0x80008000u) | bits[k] | ((top - 0x10001u * kLow) & ~top);
+        }
+        bool odd = (odd_bits & 0x80008000u) != 0u;
         if (__any_sync(kFull, raise || odd)) {
-            raise_top(x);
-            against();
+            if (__any_sync(kFull, raise)) {
+                raise_top(x);
+                against();
+            }
+            odd = false;
+#pragma unroll
+            for (int k = 0; k < NG / 2; k++)
+                odd = odd || (bits[k] & 0xc000c000u) || (bits[k] & 0xffffu) - 1u < kLow - 1u || (bits[k] >> 16) - 1u < kLow - 1u;
             odd = __any_sync(kFull, odd);
         } else {
             odd = false;
@@ -513,10 +524,6 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                     zo[t][3] += x[t][h][1] + x[t][h][3];
                 }
             }
-        float unit[NT][2];  // of the rows' products, if odd
-#pragma unroll
-        for (int t = 0; t < NT; t++) unit[t][0] = unit[t][1] = 1.0f;
-        if (odd) span_units(par, __all_sync(kFull, tiny), x, vs, unit);
         // ---- values: tokens T(2j), T(2j + 1) and those + 8, channels 4g .. 4g + 3 of each group
         uint32_t va[H][NG], vb[H][NG];
 #pragma unroll
@@ -575,137 +582,108 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                 }
             }
         }
+        if (odd) values<MASKED, true>(va, vb, vs, b, bl);
+        else values<MASKED, false>(va, vb, vs, b, bl);
+    }
+
+    // The weighted codes of a span. ODD: the products of a group are computed in fp32 and rounded to fp16
+    // in units of a power of two per row and group, in which the row's largest product in the span lies in
+    // [2^13, 2^14). Probabilities are up to 2^14, so a product with a scale of 2 and more could
+    // pass fp16, and with small scales the products would sink under its smallest numbers. The product and not the
+    // scale decides: a large value that a row gives no weight leaves its other tokens as they are.
+    template <bool MASKED, bool ODD>
+    __device__ __forceinline__ void values(const uint32_t (&va)[kSpan / kTile][NG], const uint32_t (&vb)[kSpan / kTile][NG],
+                                           const uint32_t (&vs)[kSpan / kTile][4][NG / 2],
+                                           const uint32_t (&b)[NT][kSpan / kTile][2],
+                                           const uint32_t (&bl)[NT][EXACT ? kSpan / kTile : 1][2])
+    {
+        constexpr int H = kSpan / kTile;
+        constexpr bool FRESH = EXACT || ODD;  // a tile's products are summed from 0, and added in fp32
 #pragma unroll
         for (int gr = 0; gr < NG; gr++) {
+            const uint32_t sel = (gr & 1) ? 0x7632 : 0x5410;
+            auto scales = [&](int h, int i) { return __byte_perm(vs[h][2 * i][gr / 2], vs[h][2 * i + 1][gr / 2], sel); };
+            auto product = [&](int t, int h, int i) {  // in fp32, of the lane's row and two tokens
+                float2 p = floats_of(b[t][h][i]);
+                const float2 sc = floats_of(scales(h, i));
+                if constexpr (EXACT) {
+                    const float2 r = floats_of(bl[t][h][i]);
+                    p = make_float2(p.x + r.x, p.y + r.y);
+                }
+                return make_float2(p.x * sc.x, p.y * sc.y);
+            };
+            float unit[NT], back[NT][2];  // factor of the lane's row's products; of the sums of columns 2j, 2j + 1
+            if constexpr (ODD) {
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    float m = 0.0f;  // (fmaxf passes over NaN)
+#pragma unroll
+                    for (int h = 0; h < H; h++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const float2 v = product(t, h, i);
+                            m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
+                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+                    // 2^-48 .. 2^31
+                    const int e = m > 0.0f ? min(max((int)(__float_as_uint(m) >> 23) - 127 - 13, -62), 18) : 0;
+                    unit[t] = pow2(-e);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) back[t][i] = pow2(__shfl_sync(kFull, e, (2 * (int)(threadIdx.x & 3) + i) * 4));
+                }
+            }
 #pragma unroll
             for (int h = 0; h < H; h++) {
                 uint32_t ra[4], rb[4];
                 unpack<EXACT>(va[h][gr], ra);
                 unpack<EXACT>(vb[h][gr], rb);
-                const uint32_t sel = (gr & 1) ? 0x7632 : 0x5410;
-                __half2 sc[2];
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                    sc[i] = as_half2(__byte_perm(vs[h][2 * i][gr / 2], vs[h][2 * i + 1][gr / 2], sel));
 #pragma unroll
                 for (int t = 0; t < NT; t++) {
                     uint32_t u[2], l[2];
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const __half2 p = as_half2(b[t][h][i]), ps = __hmul2(p, sc[i]);
-                        u[i] = *reinterpret_cast<const uint32_t *>(&ps);
                         l[i] = 0u;
-                        if constexpr (EXACT) {
-                            const __half2 rest = __hfma2(as_half2(bl[t][h][i]), sc[i], __hfma2(p, sc[i], __hneg2(ps)));
-                            l[i] = *reinterpret_cast<const uint32_t *>(&rest);
+                        if constexpr (ODD) {
+                            float2 v = product(t, h, i);
+                            v = make_float2(v.x * unit[t], v.y * unit[t]);
+                            u[i] = half2_of(v.x, v.y);
+                            if constexpr (EXACT) {
+                                const float2 w = floats_of(u[i]);
+                                l[i] = half2_of(v.x - w.x, v.y - w.y);
+                            }
+                        } else {
+                            const __half2 p = as_half2(b[t][h][i]), sc = as_half2(scales(h, i)), ps = __hmul2(p, sc);
+                            u[i] = *reinterpret_cast<const uint32_t *>(&ps);
+                            if constexpr (EXACT) {
+                                const __half2 rest = __hfma2(as_half2(bl[t][h][i]), sc, __hfma2(p, sc, __hneg2(ps)));
+                                l[i] = *reinterpret_cast<const uint32_t *>(&rest);
+                            }
                         }
                         if (MASKED) {
                             // a token behind a row's limit does not enter it, whatever its values are
-                            const uint32_t seen = ~__heq2_mask(p, as_half2(0u));
+                            const uint32_t seen = ~__heq2_mask(as_half2(b[t][h][i]), as_half2(0u));
                             u[i] &= seen;
                             l[i] &= seen;
                         }
                     }
 #pragma unroll
                     for (int k = 0; k < 2; k++) {
-                        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // EXACT: the tile's sum, added in fp32
-                        float(&o)[4] = EXACT ? w : O[t][gr][k];
+                        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float(&o)[4] = FRESH ? w : O[t][gr][k];
                         if constexpr (EXACT) mma_f16(o, ra[2 * k], ra[2 * k + 1], rb[2 * k], rb[2 * k + 1], l[0], l[1]);
                         mma_f16(o, ra[2 * k], ra[2 * k + 1], rb[2 * k], rb[2 * k + 1], u[0], u[1]);
-                        if constexpr (EXACT) {
+                        if constexpr (FRESH) {
 #pragma unroll
-                            for (int i = 0; i < 4; i++) O[t][gr][k][i] += w[i];
+                            for (int i = 0; i < 4; i++) {
+                                if constexpr (ODD) O[t][gr][k][i] = fmaf(w[i], back[t][i & 1], O[t][gr][k][i]);
+                                else O[t][gr][k][i] += w[i];
+                            }
                         }
                     }
                 }
             }
         }
-        if (odd) {
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                scale_sums(t, unit[t][0], unit[t][1]);
-#pragma unroll
-                for (int i = 0; i < (EXACT ? 2 : 4); i++) zo[t][i] *= fmaxf(unit[t][i & 1], 1.0f);  // a lift is not in these
-            }
-        }
-    }
-
-    // Units of a span whose V scales are unusual. Probabilities are up to 2^14, so a product with a scale
-    // of 2 and more can pass fp16: the probabilities of a row are taken in units of 2^e, its
-    // largest product in the span then under 2^15 (the product and not the scale decides: a
-    // large value that a row gives no weight leaves its other tokens as they are). If all
-    // scales are under 2^-11, they are lifted by 2^8, or products would sink under fp16's
-    // smallest numbers. The sums are brought to those units, and after the span back again.
-    __device__ __forceinline__ void span_units(const uint8_t *par, bool tiny, float (&x)[NT][kSpan / kTile][4],
-                                               uint32_t (&vs)[kSpan / kTile][4][NG / 2], float (&unit)[NT][2])
-    {
-        constexpr int H = kSpan / kTile;
-        const int t0 = token_of_row((threadIdx.x & 31) >> 2);
-        if (tiny) {
-#pragma unroll
-            for (int t = 0; t < NT; t++) unit[t][0] = unit[t][1] = 0x1p-8f;
-            const __half2 f = __float2half2_rn(256.0f);
-#pragma unroll
-            for (int h = 0; h < H; h++)
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int k = 0; k < NG / 2; k++) {
-                        const __half2 v = __hmul2(as_half2(vs[h][i][k]), f);
-                        vs[h][i][k] = *reinterpret_cast<const uint32_t *>(&v);
-                    }
-        } else {
-            float top[NT][2] = {};
-#pragma unroll
-            for (int h = 0; h < H; h++)
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const uint8_t *p = par + (h * kTile + t0 + 8 * i) * Q4<D>::PB + Q4<D>::PB / 2;
-                    float v = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < NG / 2; k++) {
-                        const float2 w = floats_of(*reinterpret_cast<const uint32_t *>(p + 4 * k));
-                        v = fmaxf(v, fmaxf(w.x, w.y));
-                    }
-                    // (a masked token's probability is 0: 0, or NaN, which fmaxf passes over)
-#pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        top[t][0] = fmaxf(top[t][0], x[t][h][2 * i] * v);
-                        top[t][1] = fmaxf(top[t][1], x[t][h][2 * i + 1] * v);
-                    }
-                }
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    float m = top[t][i];
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                    const int e = min(max((int)(__float_as_uint(m) >> 23) - 127 - 14, 0), 17);
-                    unit[t][i] = pow2(e);
-#pragma unroll
-                    for (int h = 0; h < H; h++) {
-                        x[t][h][i] *= pow2(-e);
-                        x[t][h][i + 2] *= pow2(-e);
-                    }
-                    zo[t][i] *= pow2(-e);
-                    if (!EXACT) zo[t][i + 2] *= pow2(-e);
-                }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; t++) scale_sums(t, 1.0f / unit[t][0], 1.0f / unit[t][1]);
-    }
-    __device__ __forceinline__ void scale_sums(int t, float f0, float f1)
-    {
-#pragma unroll
-        for (int gr = 0; gr < NG; gr++)
-#pragma unroll
-            for (int u = 0; u < 2; u++) {
-                O[t][gr][u][0] *= f0;
-                O[t][gr][u][2] *= f0;
-                O[t][gr][u][1] *= f1;
-                O[t][gr][u][3] *= f1;
-            }
     }
 
     // A logit passed the running maximum by the slack (rare): a new reference.
