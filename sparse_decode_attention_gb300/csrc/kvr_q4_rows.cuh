@@ -582,8 +582,8 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                 }
             }
         }
-        if (odd) values<MASKED, true>(va, vb, vs, b, bl);
-        else values<MASKED, false>(va, vb, vs, b, bl);
+        if (odd) values<MASKED, true>(va, vb, vs, b, bl, live, base);
+        else values<MASKED, false>(va, vb, vs, b, bl, live, base);
     }
 
     // The weighted codes of a span. ODD: the products of a group are computed in fp32 and rounded to fp16
@@ -595,9 +595,21 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     __device__ __forceinline__ void values(const uint32_t (&va)[kSpan / kTile][NG], const uint32_t (&vb)[kSpan / kTile][NG],
                                            const uint32_t (&vs)[kSpan / kTile][4][NG / 2],
                                            const uint32_t (&b)[NT][kSpan / kTile][2],
-                                           const uint32_t (&bl)[NT][EXACT ? kSpan / kTile : 1][2])
+                                           const uint32_t (&bl)[NT][EXACT ? kSpan / kTile : 1][2],
+                                           uint32_t live, int base)
     {
         constexpr int H = kSpan / kTile;
+        const int g = (threadIdx.x & 31) >> 2, ta = token_of_row(2 * (threadIdx.x & 3)), tb = token_of_row(2 * (threadIdx.x & 3) + 1);
+        uint32_t seen[NT];  // the tokens that row g of a block sees
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            seen[t] = live;
+            if (MASKED && ODD) {
+                const int even = __shfl_sync(kFull, lim[t][0], g >> 1), other = __shfl_sync(kFull, lim[t][1], g >> 1);
+                const int n = ((g & 1) ? other : even) - base;
+                seen[t] = live & (n <= 0 ? 0u : n >= kSpan ? 0xffffffffu : (1u << n) - 1u);
+            }
+        }
         constexpr bool FRESH = EXACT || ODD;  // a tile's products are summed from 0, and added in fp32
 #pragma unroll
         for (int gr = 0; gr < NG; gr++) {
@@ -660,11 +672,13 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                                 l[i] = *reinterpret_cast<const uint32_t *>(&rest);
                             }
                         }
-                        if (MASKED) {
-                            // a token behind a row's limit does not enter it, whatever its values are
-                            const uint32_t seen = ~__heq2_mask(as_half2(b[t][h][i]), as_half2(0u));
-                            u[i] &= seen;
-                            l[i] &= seen;
+                        if (MASKED && ODD) {  // (NaN scales are odd)
+                            // a token that the row does not see does not enter it, whatever its values are; one that
+                            // it sees does, a NaN of a probability of 0 too
+                            const uint32_t two = seen[t] >> (h * kTile + 8 * i);
+                            const uint32_t enter = ((two >> ta) & 1u ? 0xffffu : 0u) | ((two >> tb) & 1u ? 0xffff0000u : 0u);
+                            u[i] &= enter;
+                            l[i] &= enter;
                         }
                     }
 #pragma unroll

@@ -103,3 +103,33 @@ def test_scales_of_every_size_token_by_token(ot, d):
         want = q4.attend_row(qn, K, V, 0.1)
         tol = product_tolerance(b, K, V, qn, 0.1, ot, want)
         assert np.all(np.abs(o[0, g].double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("ot", [F32, BF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [64, 90, 899, 3000])
+def test_a_nan_value_of_a_vanishing_probability(ot, d, N):
+    """0 times NaN is NaN: a row that sees such a token has it, wherever the token lies; a row that does not, has not."""
+    ps, Lq, NG = 32, 3, d // 32
+    spots = {0, 17, 31, 32, N - 26, N - 4, N - 3, N - 1}
+    for tok in sorted(t for t in spots if 0 <= t < N):
+        b = Batch([N], 1, ps, d, seed=35)
+        p = params(b)[b.table[0, tok // ps], 0, tok % ps]
+        p[0], p[1] = 0.0, -100.0                    # a logit 100s under the others
+        p[2, NG - 1], p[3, NG - 1] = np.nan, np.nan  # as kvr_append_q4 writes a group that fp16 cannot hold
+        b.pages.copy_(torch.from_numpy(b.np_pages))
+        for G in (1, 4):
+            q = torch.ones((1, Lq, G, d), dtype=BF, device=DEV)
+            want = np.zeros((Lq, G, d), bool)
+            for t in range(Lq):
+                if tok <= N - Lq + t:
+                    want[t, :, 32 * (NG - 1):] = True
+            for o in b.attend(q, ot, 0.1):
+                assert np.array_equal(torch.isnan(o[0]).cpu().numpy(), want), (tok, G)
+        idx = np.arange(0, N - 20, 3, dtype=np.int32)[None, None]
+        o = torch.zeros((1, 4, d), dtype=ot, device=DEV)
+        kvr.kvr_sparse_attend_q4(b.cache, torch.ones((1, 4, d), dtype=BF, device=DEV), i32(b.table), i32(idx),
+                                 i32([[idx.size]]), i32([N]), 20, 0.1, o, b.ws(1, 4))
+        seen = tok in q4.token_list(idx[0, 0], idx.size, N, 20)
+        bad = torch.isnan(o[0]).cpu().numpy()
+        assert not bad[:, :32 * (NG - 1)].any() and (bad[:, 32 * (NG - 1):] == seen).all(), tok
