@@ -32,6 +32,8 @@
 // fl(lo s + (hi s - u)) beside it, the bracket exact as a fused multiply-add.
 #pragma once
 
+#include <cfloat>
+
 #include "kvr_paged.h"
 #include "kvr_q4.cuh"
 
@@ -44,7 +46,7 @@ namespace q4a {
 constexpr int kTile = 16;                // tokens of a tile
 constexpr int kSpan = 2 * kTile;         // tokens that a warp takes at once
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kEmpty = -3.0e38f;       // running maximum before the first token
+constexpr float kEmpty = -FLT_MAX;       // largest score before the first token
 constexpr float kSlack = 3.0f;           // logits (log2) may pass the running maximum by this much
 constexpr float kExp = 11.0f;            // log2 of the largest token's probability as it is kept
 static_assert(kExp + kSlack + 1.0f <= 15.0f, "fp16's range, times a scale under 2");
@@ -173,10 +175,12 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     static constexpr int FOLD = EXACT ? INT32_MAX : 32;
 
     // Scores are kept as x with logit (log2) = x * kq, kq > 0. Probabilities are
-    // 2^(x kq - ref) with ref = (largest x so far) kq - kExp: up to 2^14.
+    // 2^((x - top) kq + kExp), top the largest x so far or a little less: up to 2^14. The difference comes
+    // first: x kq - (top kq - kExp) would round the reference at the logits' size, and from 2^27 on
+    // the largest token itself to 0 or past fp16.
     // [NT]: blocks of 8 rows.
     uint32_t qf[NT][NG][4], ql[NT][Q2 ? NG : 1][4], qz[NT][2];
-    float kq[NT][2], ref[NT][2], kept[NT][2], O[NT][NG][2][4];
+    float kq[NT][2], top[NT][2], kept[NT][2], O[NT][NG][2][4];
     // [0], [1]: row gr, sum of p z of group gr; [2], [3]: sum of p, which the other rows of the same
     // product give (a million tokens, bf16: 249 -> 241 us); EXACT, where a product's sums are added
     // in fp32 (342 us so, 333), this lane's tokens
@@ -299,13 +303,13 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
         }
         const int ke = -up;  // -139 .. 114, in two factors
         // (below 2^-110 all logits vanish: x is under 2^50, and a factor of 0 would make a masked
-        // score's -inf a NaN)
-        const float k = kscale == 0.0f ? 1.0f : fmaxf(kscale * pow2(ke >> 1) * pow2(ke - (ke >> 1)), 0x1p-110f);
+        // score's -inf a NaN, as an infinite one a difference of 0)
+        const float k = kscale == 0.0f ? 1.0f : fminf(fmaxf(kscale * pow2(ke >> 1) * pow2(ke - (ke >> 1)), 0x1p-110f), FLT_MAX);
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             kq[t][i] = __shfl_sync(kFull, k, (2 * j + i) * 4);
             lim[t][i] = causal ? N - a.Lq + 1 + min(r0 + 2 * j + i, a.R - 1) / a.G : INT32_MAX;
-            ref[t][i] = kept[t][i] = kEmpty;
+            top[t][i] = kept[t][i] = kEmpty;
 #pragma unroll
             for (int gr = 0; gr < NG; gr++)
 #pragma unroll
@@ -316,7 +320,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     }
 
     // The sums of the last tiles added to the merge rows (which hold the
-    // earlier ones against the reference `kept`).
+    // earlier ones against `kept`).
     __device__ __forceinline__ void fold()
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
@@ -325,8 +329,8 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
         for (int t = 0; t < NT; t++) {
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                const float f = ex2(kept[t][i] - ref[t][i]);
-                kept[t][i] = ref[t][i];
+                const float f = ex2((kept[t][i] - top[t][i]) * kq[t][i]);
+                kept[t][i] = top[t][i];
 #pragma unroll
                 for (int gr = 0; gr < NG; gr++) {
                     float(&o)[2][4] = O[t][gr];
@@ -346,7 +350,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                 }
                 if (g == 0) {
                     float2 *p = stat + (threadIdx.x >> 5) * RT + 8 * t + 2 * j + i;
-                    *p = make_float2(ref[t][i], folds > 0 ? fmaf(p->y, f, l) : l);
+                    *p = make_float2(fmaf(top[t][i], kq[t][i], -kExp), folds > 0 ? fmaf(p->y, f, l) : l);
                 }
             }
             zo[t][0] = zo[t][1] = zo[t][2] = zo[t][3] = 0.0f;
@@ -473,7 +477,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
 #pragma unroll
                 for (int h = 0; h < H; h++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) y[t][h][i] = fmaf(x[t][h][i], kq[t][i & 1], -ref[t][i & 1]);
+                    for (int i = 0; i < 4; i++) y[t][h][i] = fmaf(x[t][h][i] - top[t][i & 1], kq[t][i & 1], kExp);
         };
         against();
         float over = y[0][0][0];
@@ -700,7 +704,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
         }
     }
 
-    // A logit passed the running maximum by the slack (rare): a new reference.
+    // A logit passed the running maximum by the slack (rare): a new one.
     __device__ __forceinline__ void raise_top(const float (&x)[NT][kSpan / kTile][4])
     {
 #pragma unroll
@@ -710,10 +714,10 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
                 float m = fmaxf(fmaxf(x[t][0][i], x[t][0][i + 2]), fmaxf(x[t][1][i], x[t][1][i + 2]));
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                const float r = fmaxf(m > kEmpty ? fmaf(m, kq[t][i], -kExp) : kEmpty, ref[t][i]);
-                // nothing summed yet: the old reference may be any
-                const float f = ref[t][i] == kEmpty ? 0.0f : ex2(ref[t][i] - r);
-                ref[t][i] = r;
+                const float r = fmaxf(m, top[t][i]);
+                // nothing summed yet: the old one may be any
+                const float f = top[t][i] == kEmpty ? 0.0f : ex2((top[t][i] - r) * kq[t][i]);
+                top[t][i] = r;
                 zo[t][i] *= f;
                 zo[t][i + 2] *= f;
 #pragma unroll

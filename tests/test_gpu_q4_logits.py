@@ -88,3 +88,43 @@ def test_queries_of_extreme_size_bf16_outputs():
     q[..., 5] *= 1e6
     for o in b.attend(q, BF, 1e-7):
         b.check_dense(q, o, 1e-7)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("qt,ot", TYPES)
+@pytest.mark.parametrize("size", [2.0 ** 26, 3e8, 1e10, -1e20, 1e35])
+def test_logits_far_beyond_the_softmax_reference(d, qt, ot, size):
+    """Logits whose fp32 steps are larger than the differences a softmax sees: the largest one's value, where it
+    leads by more than their errors."""
+    b = Batch([1, 2, 33, 300, 2100], 2, 64, d, seed=19)
+    scale = size / (0.3 * d)
+    q = b.query(1, 8, qt)
+    qn, rows = q.double().cpu().numpy(), 0
+    for o in b.attend(q, ot, scale):
+        on = o.double().cpu().numpy()
+        for r, N in enumerate(b.lens):
+            for h in range(2):
+                K, V = b.kv(r, h, np.arange(N))
+                for g in range(4 * h, 4 * h + 4):
+                    x = (K @ qn[r, 0, g]) * float(np.float32(scale))
+                    A = abs(scale) * np.max(np.abs(qn[r, 0, g]) @ np.abs(K).T)
+                    at = np.argsort(x)
+                    if N > 1 and x[at[-1]] - x[at[-2]] <= 2 * 72 * U * (A + 1) + 60:
+                        continue
+                    rows += 1
+                    want, v = V[at[-1]], np.abs(V).max()
+                    R = V.reshape(N, -1, 32).max() - V.reshape(N, -1, 32).min()
+                    # one token: its probability cancels but for the roundings of the products and the quotient
+                    tol = 8 * U * v + (2.0 ** -8 * np.abs(want) + 2.0 ** -11 * (3 * R + v) if ot == BF else U * np.abs(want) + 2.0 ** -21 * (R + v))
+                    assert np.all(np.abs(on[r, 0, g] - want) <= tol), (N, g, on[r, 0, g][:4], want[:4])
+    assert rows > 40
+
+
+def test_a_zero_query_under_the_largest_scale():
+    """All logits are 0: the mean of the values."""
+    b = Batch([1, 90, 700], 1, 32, 128, seed=20)
+    for qt in (BF, F32):
+        q = torch.zeros((3, 1, 4, 128), dtype=qt, device=DEV)
+        for ot in (BF, F32):
+            for o in b.attend(q, ot, 3e38):
+                b.check_dense(q, o, 3e38)
