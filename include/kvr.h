@@ -647,7 +647,8 @@ kvr_status kvr_read_q4(const kvr_q4_cache *cache, kvr_dtype dtype, const int64_t
                        int64_t n_tokens, void *K, int64_t k_stride, void *V, int64_t v_stride,
                        int32_t *err_word, void *stream);
 
-/* Bytes of device workspace of the two attention calls below (Lq = 1 for the sparse one). */
+/* Bytes of device workspace of the two attention calls below (Lq = 1 for the sparse one, which asks for
+ * the same and leaves it as it is). */
 size_t kvr_attend_q4_workspace_size(const kvr_q4_cache *cache, int B, int Lq, int Hq);
 
 /*
@@ -670,13 +671,16 @@ size_t kvr_attend_q4_workspace_size(const kvr_q4_cache *cache, int B, int Lq, in
  *               starts at element (b * Lq + t) * q_stride, a multiple of 16
  *               bytes and at least Hq * d.
  *   block_table device int32 [B, max_pages]; an entry outside the pool sets
- *               KVR_DEVERR_PAGE and its tokens are skipped.
+ *               KVR_DEVERR_PAGE and its tokens are skipped. Lengths are not known on the host, so
+ *               max_pages * page_size is taken for the longest: short requests are
+ *               faster under a table that is no wider than they need.
  *   seq_len     device int32 [B]; a value outside [0, max_pages * page_size]
  *               sets KVR_DEVERR_SEQ_LEN and counts as 0.
  *   scale       finite, else KVR_ERR_INVALID_ARG.
  *   out         device [B, Lq, Hq, d] of out_dtype (written). With KVR_BF16 the
- *               probabilities times scales enter the second product as fp16,
- *               with KVR_F32 as a sum of two.
+ *               probabilities (which, so rounded, the softmax divides by) and their
+ *               products with scales are rounded to fp16, and codes enter the second product
+ *               to 2^-16 of its sum; with KVR_F32 both are sums of two fp16 terms.
  *   workspace   >= kvr_attend_q4_workspace_size bytes, 256-byte aligned;
  *               contents on entry are ignored; calls that run at the same time
  *               need one each.

@@ -11,12 +11,14 @@
 // the workspace, which combine_q4_kernel merges in the order of the CTAs: the
 // same bits every time.
 //
-// A million tokens of 8 KV heads, d = 128, bf16: 241 us, 5.6 TB/s (0.82 of the
+// A million tokens of 8 KV heads, d = 128, bf16: 238 us, 5.6 TB/s (0.83 of the
 // measured copy); copies without the computation take 195 us, the computation without
-// the copies 229 us. So the instructions bound it (half of the issue slots, 46% of the
-// integer pipe at three warps a scheduler), as they do more with fp32 outputs (333 us).
-// 128K tokens: 41 us, of which 4.6 us go by until the first chunk has landed
-// and 3.7 us after the last, in the two merges and the second launch.
+// the copies took 229 us. So the computation bounds it, but by latency and not by a unit that is full:
+// three warps a scheduler use half of the issue slots and 46% of the integer pipe, and wait for operands,
+// shared memory and the tensor pipe (20%) in between. With fp32 outputs it is 321 us, with fp32 queries 358.
+// 128K tokens: 43 us, of which 4.6 us go by until the first chunk has landed
+// and 3.7 us after the last, in the two merges and the second launch. A unit that is opened and closed
+// costs some 3 us of a CTA: 60000 requests of 16 tokens, one KV head, take 2.4 ms.
 #pragma once
 
 #include <algorithm>
@@ -28,8 +30,8 @@ namespace q4a {
 
 // One warp issues a bulk copy in about 50 ns, three a page. Pages of 64 tokens and more leave it
 // idle part of a chunk's time (1.2 us at the bandwidth of memory). Of smaller ones every
-// warp copies its own 32 tokens, 16 bytes a lane: a million tokens (bf16) in pages of 32 take 281 us
-// so, in pages of 64 257 us, and 281 if the warps copied those too. (With bulk copies of the
+// warp copies its own 32 tokens, 16 bytes a lane: a million tokens (bf16) in pages of 32 take 288 us
+// so, in pages of 64 272 us, and 287 if the warps copied those too. (With bulk copies of the
 // warps' own, pages of 32 took 15% longer.)
 constexpr int kOwnCopies = 32;              // pages of up to so many tokens
 
@@ -547,10 +549,10 @@ inline size_t dense_ws_bytes(int d)
 
 // Query rows go 8 at a time, or as two blocks of 8 that share the unpacked codes, in a warp of 255
 // registers, seven of them an SM (fp32 queries at d = 128 would need more). A pair takes so much
-// longer than a block, in tenths: 12 requests of 16K tokens, 4 KV heads, 16 rows in pairs and by
-// blocks: d = 64 38 and 55 us (fp32 outputs 46 and 60, fp32 queries 49 and 58), d = 128 50 and 60 (70
-// and 76); 24 rows: 66 and 77 (81 and 84, 87 and 81), 86 and 84; 56 rows, d = 128: 161 and 179 (241 and
-// 233). (At 12 warps an SM the pair spills: 133 us for what took 102 by blocks then.)
+// longer than a block, in tenths: 12 requests of 16K tokens, 4 KV heads, pages of 64, 16 rows in pairs and by
+// blocks: d = 64 39 and 55 us (fp32 outputs 45 and 60, fp32 queries 48 and 58), d = 128 51 and 63 (69
+// and 74); 24 rows: 67 and 77 (78 and 85, 83 and 81), 87 and 88 (125 and 104); 56 rows, d = 128: 162 and
+// 187 (237 and 224). (At 12 warps an SM the pair spills: 133 us for what took 102 by blocks then.)
 constexpr int pair_cost(int d, bool q2, bool exact) { return d == 64 ? (q2 ? 17 : 14) : exact ? 18 : 16; }
 
 template <int D>

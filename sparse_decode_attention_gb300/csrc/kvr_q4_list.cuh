@@ -15,9 +15,8 @@
 //
 // What bounds it is the chain of dependent reads (length, list, page, rows: 0.6, 1.0 and
 // 0.9 us), then the products (0.5 us), the two merges and the barrier (2 us). 2048 selected
-// tokens and a window of 128 of a 128K request (8 KV heads): 7.5 us in a graph,
-// for 0.4 us of bytes. With 16 CTAs a unit, of which seven clusters and not eight are
-// resident, it took 14.3 us.
+// tokens and a window of 128 of a 128K request (8 KV heads): 8.2 us, for 0.4 us of bytes. With 16 CTAs a
+// unit, of which seven clusters and not eight are resident, it took 14.3 us for 7.5 at that time.
 #pragma once
 
 #include <algorithm>
@@ -35,14 +34,16 @@ constexpr int kFewWarps = 4;    // of a CTA of which three share an SM
 constexpr int kMaxCluster = 16;
 // Spans of a warp up to which all tokens of a request go this way rather than through
 // the dense kernel, which needs a second one to merge. bf16, d = 128, this way and that:
-// 8 units of 4096 tokens (one span) 7.8 and 9.7 us, 64 of 2048 (three) 11.4 and 14.1,
-// 128 of 1024 (three) 9.7 and 15.1; of four spans, 8 units of 16000 13.7 and 12.7.
+// 8 units of 4096 tokens (one span) 8.4 and 10.0 us, 64 of 2048 (three) 12.4 and 14.6,
+// 128 of 1024 (three) 10.6 and 15.5; of four spans, 8 units of 16000 14.6 and 13.3.
+// (The lengths are on the device, so what counts is what the page table has room for: short requests under a
+// wide table go the other way.)
 constexpr int kListSteps = 3;
 
 // With more units than SMs a unit is a CTA of four warps, three to an SM, while its list gives a warp
-// no more spans than this. bf16, d = 128, 192 units: 120 tokens 6.6 us so and 11.3 through the dense
-// kernel, 380 9.8 and 15.3, 1000 16.9 and 19.3, 1400 (12 spans) both 22.2; 3200 units of 380 tokens 78 and
-// 125. Selected tokens, and with CTAs of 12 warps: 192 lists of 428 11.6 and 15.3, of 1128 22.4 and 24.9.
+// no more spans than this. bf16, d = 128, 192 units: 120 tokens 6.7 us so and 11.4 through the dense
+// kernel, 380 9.0 to 10.9 and 15.8, 1000 17.4 and 19.7, 1400 (12 spans) both 22.6; 3200 units of 380 tokens 81
+// and 128. Selected tokens, and with CTAs of 12 warps: 192 lists of 428 11.7 and 15.5, of 1128 23.4 and 26.0.
 constexpr int kFewSteps = 10;
 
 struct ListArgs : Args {
