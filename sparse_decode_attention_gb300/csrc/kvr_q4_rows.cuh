@@ -58,7 +58,7 @@ struct Args {
     int64_t q_stride, max_pages, cap;
     const void *q;
     const int32_t *table, *seq_len;
-    float scale_log2;
+    float scale;
     void *out;
     int out_bf16;
     int32_t *err;
@@ -236,7 +236,7 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
     {
         const int lane = threadIdx.x & 31, j = lane & 3;
         // the sign of the scale goes into the query; scale 0 makes the query 0
-        const float kscale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.0f ? -1.0f : a.scale_log2 > 0.0f ? 1.0f : 0.0f;
+        const float kscale = fabsf(a.scale), sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
         if (t == 0) lim_min = causal ? N - a.Lq + 1 + r0 / a.G : INT32_MAX;
         float (&x)[NG][8] = q;
         float amax = 0.0f, odd = 0.0f;
@@ -301,10 +301,11 @@ template <int D, bool Q2, bool EXACT, int WARPS, int NT> struct Rows {
             qz[t][0] = j == 0 ? part[0][0] : j == 1 ? part[1][0] : j == 2 ? part[2][0] : 0u;
             qz[t][1] = 0u;
         }
+        // (log2 e comes last: with a scale of 3e38 it would pass fp32, whatever the query)
         const int ke = -up;  // -139 .. 114, in two factors
         // (below 2^-110 all logits vanish: x is under 2^50, and a factor of 0 would make a masked
         // score's -inf a NaN, as an infinite one a difference of 0)
-        const float k = kscale == 0.0f ? 1.0f : fminf(fmaxf(kscale * pow2(ke >> 1) * pow2(ke - (ke >> 1)), 0x1p-110f), FLT_MAX);
+        const float k = kscale == 0.0f ? 1.0f : fminf(fmaxf(kscale * pow2(ke >> 1) * pow2(ke - (ke >> 1)) * kLog2e, 0x1p-110f), FLT_MAX);
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             kq[t][i] = __shfl_sync(kFull, k, (2 * j + i) * 4);
@@ -771,7 +772,7 @@ inline Args make_args(const kvr_q4_cache &c, const Q4AttendArgs &s, int RT)
     a.q = s.q;
     a.table = s.table;
     a.seq_len = s.seq_len;
-    a.scale_log2 = s.scale * kLog2e;
+    a.scale = s.scale;
     a.out = s.out;
     a.out_bf16 = s.out_dtype == KVR_BF16;
     a.err = s.err;

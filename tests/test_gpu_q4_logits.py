@@ -128,3 +128,13 @@ def test_a_zero_query_under_the_largest_scale():
         for ot in (BF, F32):
             for o in b.attend(q, ot, 3e38):
                 b.check_dense(q, o, 3e38)
+
+
+def test_the_largest_scales_of_the_smallest_queries():
+    """Ordinary logits of a scale of 3.3e38, which times log2 e would pass fp32."""
+    b = Batch([1, 90, 700], 2, 32, 128, seed=22)
+    for qt in (BF, F32):
+        q = (b.query(2, 8, F32).double() * 1e-39).to(qt)
+        for ot in (BF, F32):
+            for o in b.attend(q, ot, 3.3e38):
+                b.check_dense(q, o, 3.3e38)
