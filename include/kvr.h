@@ -660,14 +660,16 @@ size_t kvr_attend_q4_workspace_size(const kvr_q4_cache *cache, int B, int Lq, in
  *   out[b, t, g, :] = sum_{i <= N - Lq + t} softmax_i(scale * q . k_i) v_i
  * over the cached values k_i, v_i; a row without tokens (N - Lq + t < 0) is 0.
  * Sums are kept in fp32: a score is off by less than 2^-17 of
- * |scale| sum_c |q_c| (s code_c + |z|). A query's channels are held to 2^-34 of the row's largest, their
- * sums over a group (which multiply z) to 2^-32 of it, and those of an fp32 query to 2^-22
- * of their own size. A query row that is not finite gives NaN, and so may one
- * whose scores (times log2 e) pass fp32's range. Keys and values that a row does not see, whatever
- * they hold, do not enter it; a NaN among those that it sees does, however small its probability. A token's probability is held to 2^-36 of the row's
- * largest, P, beside its own rounding; its product with a scale of its values to 2^-36 P,
- * and where the scales of a group are all under 2^-11 (KVR_F32: 2^-7) in 32 consecutive tokens of the
- * list, or one is 2 or more, to 2^-38 of the row's largest such product among these tokens.
+ * |scale| sum_c |q_c| (s code_c + |z|). A query's channels are held to 2^-34 of the
+ * row's largest, their sums over a group (which multiply z) to 2^-32 of it, and those
+ * of an fp32 query to 2^-22 of their own size. A query row that is not finite gives
+ * NaN, and so may one whose scores (times log2 e) pass fp32's range. Keys and values
+ * that a row does not see, whatever they hold, do not enter it; a NaN among those that
+ * it sees does, however small its probability. A token's probability is held to 2^-36
+ * of the row's largest, P, beside its own rounding; its product with a scale of its
+ * values to 2^-36 P, and where the scales of a group are all under 2^-11 (KVR_F32: 2^-7)
+ * in 32 consecutive tokens of the list, or one is 2 or more, to 2^-38 of the row's
+ * largest such product among these tokens.
  *   q           device [B, Lq, Hq, d] of q_dtype, 16-byte aligned; row (b, t)
  *               starts at element (b * Lq + t) * q_stride, a multiple of 16
  *               bytes and at least Hq * d.
